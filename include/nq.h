@@ -458,8 +458,9 @@ int nq_cache_read(const nq_kv_cache* cache, const int32_t* slots, int64_t tokens
  * precision).  The result does not depend on timing (pieces are merged in
  * order).
  * workspace: device scratch of nq_tree_attention_workspace_bytes(...) for the
- * same arguments, 16-byte aligned, any contents (may be NULL if that is 0); calls
- * sharing one must be ordered.
+ * same arguments or for more sequences and drafted tokens in all (seqs, total),
+ * 16-byte aligned, any contents (may be NULL if that is 0); calls sharing one must
+ * be ordered.
  * Found by the kernel, reported by nq_last_device_error as NQ_ERANGE: a page
  * outside the cache (its keys are not seen), a sequence whose length is
  * negative or that passes table_width pages (cut there), more drafted tokens
@@ -471,7 +472,8 @@ int nq_tree_attention(const nq_kv_cache* cache, const void* q, int64_t q_token_s
                       int seqs, int max_drafts, int64_t max_context, float scale, void* out,
                       float* lse, void* workspace, size_t workspace_bytes, nq_stream_t stream);
 
-/* Bytes of workspace nq_tree_attention needs on the current device. */
+/* Bytes of workspace nq_tree_attention needs on the current device for batches
+ * of up to seqs sequences (the other arguments as in the call). */
 int nq_tree_attention_workspace_bytes(int seqs, int max_drafts, int64_t total, int q_heads,
                                       int kv_heads, int head_dim, int64_t max_context,
                                       size_t* bytes);

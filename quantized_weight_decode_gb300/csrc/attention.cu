@@ -522,6 +522,9 @@ struct AttnPlan {
   size_t bytes, ml_at, units_at;  // of the workspace; words before the (reference, sum) pairs, the units' blocks
 };
 
+// At most this many keys over all kv heads take the few-rows kernel to 64 rows.
+constexpr int64_t kFewKeys = 16384;
+
 // Which kernel: few rows up to 16 (two of its row blocks), to 32 for heads of
 // 64 channels.  Measured on both sides (us, few / many; 8 sequences of 8 k,
 // 18 to 36 rows): heads of 128, 48.1 / 44.6 to 67.3 / 50.0; of 256, 47.9 / 45.2 to
@@ -531,7 +534,7 @@ struct AttnPlan {
 // 15.7 / 16.5 (128), 13.5 / 18.8 to 16.0 / 27.0 (256), 11.1 / 12.6 to 12.9 / 15.7 (64).
 bool takes_many(int rows, int dim, int64_t keys) {
   if (rows <= (dim == 64 ? 32 : 16)) return false;
-  return rows > 64 || keys > 16384;
+  return rows > 64 || keys > kFewKeys;
 }
 
 AttnPlan plan_attention(int sms, int seqs, int max_drafts, int q_heads, int kv_heads, int dim,
@@ -564,6 +567,21 @@ AttnPlan plan_attention(int sms, int seqs, int max_drafts, int q_heads, int kv_h
   p.units_at = p.ml_at + pieces * 2;
   p.bytes = p.blocks == 1 ? 0 : (p.units_at + static_cast<size_t>(units) * 2) * sizeof(float);
   return p;
+}
+
+// Workspace of every batch of up to `seqs` sequences.  Within one kernel it grows
+// with the batch, but a smaller batch may take the few-rows kernel instead, which
+// has more blocks: the largest such batch counts too.
+size_t workspace_bytes_up_to(int sms, int seqs, int max_drafts, int q_heads, int kv_heads, int dim,
+                             int64_t max_context) {
+  const AttnPlan p = plan_attention(sms, seqs, max_drafts, q_heads, kv_heads, dim, max_context);
+  size_t bytes = p.bytes;
+  const int64_t few = max_context > 0 ? kFewKeys / (max_context * kv_heads) : 0;  // sequences
+  if (p.many && few >= 1 && few < seqs) {
+    const AttnPlan f = plan_attention(sms, static_cast<int>(few), max_drafts, q_heads, kv_heads, dim, max_context);
+    bytes = std::max(bytes, f.bytes);
+  }
+  return bytes;
 }
 
 int check_attention(int seqs, int max_drafts, int q_heads, int kv_heads, int dim, int64_t total,
@@ -600,7 +618,7 @@ int nq_tree_attention_workspace_bytes(int seqs, int max_drafts, int64_t total, i
   int* status;
   int sms;
   if (int rc = device_status(&status, &sms)) return rc;
-  *bytes = plan_attention(sms, seqs, max_drafts, q_heads, kv_heads, head_dim, max_context).bytes;
+  *bytes = workspace_bytes_up_to(sms, seqs, max_drafts, q_heads, kv_heads, head_dim, max_context);
   return NQ_OK;
 }
 
