@@ -617,6 +617,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
       }
       queries_done<C::kSoftmaxThreads>();
 
+      bool unset = false;  // this lane's row (below) has no reference after the tiles so far
       for (int t = 0; t < tiles; ++t) {
         const unsigned n = done + t, slot = n % kScaleSlots;
         wait(st.scales_full[slot], n / kScaleSlots);
@@ -691,10 +692,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
               if (bad >> g & 1u) atomicOr(&st.poison[g][c >> 2], m << (8 * (c & 3)));
           }
         }
-        // A tile that may hold a row's first key moves the references too.
+        // A tile that may hold a row's first key moves the references too (tiles
+        // before it may have had none: their pages were not the cache's).
         // The four warps that share rows (one a quarter of the keys) agree among
         // themselves; the groups of warps are not in step.
-        const bool move = group_any(cg, high > kHigh || t == 0 || masked);
+        const bool move = group_any(cg, high > kHigh || t == 0 || masked || unset);
         if (n > 0) wait(st.o_full, n - 1);
         if (move) {
           const int row = 8 * (cg + C::kGroups * (lane >> 3)) + (lane & 7);  // a lane of the first warp's
@@ -723,6 +725,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
             }
             st.top[row] = __float_as_int(by);
             st.factor[row] = factor;
+            unset = row < rows && !st.set[row];
           }
           group_sync(cg);
           tcgen05_fence_after();
