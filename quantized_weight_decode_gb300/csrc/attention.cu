@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, few_blocks(D, NT)) nq_attn_few_k
   float2* sm_ml = reinterpret_cast<float2*>(sm_o + kWarpsA * R * D);
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 2, r = lane & 3;
-  const Line line(a, lane);
+  const Line line(a, lane, blockIdx.x == 0 && warp == 0);
   const long long stretch = line.stretch(a, gridDim.x);
   const long long pos_end = min(line.total, (blockIdx.x + 1) * stretch);
   long long pos = blockIdx.x * stretch;

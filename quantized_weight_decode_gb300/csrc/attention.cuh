@@ -63,8 +63,8 @@ struct SeqView {
   int len, keys;                     // committed keys; committed and drafted
 };
 
-// (report: what is wrong with it goes to the status word, by one thread)
-__device__ __forceinline__ SeqView seq_view_of(const AttnArgs& a, int s, bool report) {
+// (report: what is wrong with it goes to the status word, by every thread that asks)
+__device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s, bool report = false) {
   SeqView v;
   bool bad = false;
   long long first, n;
@@ -90,11 +90,8 @@ __device__ __forceinline__ SeqView seq_view_of(const AttnArgs& a, int s, bool re
   v.drafts = static_cast<int>(n);
   v.len = static_cast<int>(len);
   v.keys = static_cast<int>(len + n > room ? room : len + n);
-  if (report && bad && threadIdx.x == 0) atomicCAS(a.status, 0, kStatusRange);
+  if (report && bad) atomicCAS(a.status, 0, kStatusRange);
   return v;
-}
-__device__ __forceinline__ SeqView seq_view(const AttnArgs& a, int s) {
-  return seq_view_of(a, s, true);
 }
 
 // Bits of the drafted keys that drafted token t of the sequence sees.
@@ -171,7 +168,9 @@ __device__ __forceinline__ uint32_t nibbles_bf16(uint32_t w) {
 // lengths leave no block with more than another; a unit that several blocks
 // share is merged from pieces, and the piece of block b of unit u (numbered
 // over the batch) has the place b + u: along the line one of the two grows by
-// one.  Computed by whole warps.
+// one.  Computed by whole warps.  The one that a kernel builds with `report` (one
+// warp of its first block) looks at every sequence, those without rows among
+// them, and reports what is wrong with it.
 __device__ __forceinline__ long long divide_long(long long n, long long d) {  // n, d >= 0
   if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
   return n / d;
@@ -184,17 +183,18 @@ struct Place {
 struct Line {
   long long total;
   long long upto;             // tiles of the first 32 sequences, up to that of this lane
-  static __device__ __forceinline__ void seq(const AttnArgs& a, int s, int* row_tiles, int* tiles) {
-    const SeqView v = seq_view_of(a, s, false);
+  static __device__ __forceinline__ void seq(const AttnArgs& a, int s, int* row_tiles, int* tiles,
+                                             bool report = false) {
+    const SeqView v = seq_view(a, s, report);
     *row_tiles = (v.drafts * a.group + a.tile_rows - 1) / a.tile_rows;
     *tiles = max(1, (v.keys + a.tile_keys - 1) / a.tile_keys);
   }
   // Tiles of the sequences s0 .. s0 + lane.
-  static __device__ __forceinline__ long long scan(const AttnArgs& a, int s0, int lane) {
+  static __device__ __forceinline__ long long scan(const AttnArgs& a, int s0, int lane, bool report = false) {
     long long n = 0;
     if (s0 + lane < a.seqs) {
       int rt, k;
-      seq(a, s0 + lane, &rt, &k);
+      seq(a, s0 + lane, &rt, &k, report);
       n = static_cast<long long>(rt) * a.c.kv_heads * k;
     }
 #pragma unroll
@@ -204,10 +204,10 @@ struct Line {
     }
     return n;
   }
-  __device__ __forceinline__ Line(const AttnArgs& a, int lane) {
-    upto = scan(a, 0, lane);
+  __device__ __forceinline__ Line(const AttnArgs& a, int lane, bool report = false) {
+    upto = scan(a, 0, lane, report);
     total = __shfl_sync(0xffffffffu, upto, 31);
-    for (int s = 32; s < a.seqs; s += 32) total += __shfl_sync(0xffffffffu, scan(a, s, lane), 31);
+    for (int s = 32; s < a.seqs; s += 32) total += __shfl_sync(0xffffffffu, scan(a, s, lane, report), 31);
   }
   __device__ __forceinline__ long long stretch(const AttnArgs& a, int blocks) const {
     const long long n = divide_long(total + blocks - 1, blocks);

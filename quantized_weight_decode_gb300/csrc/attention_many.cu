@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
     x.live = pos < pos_end;
     if (x.live) {
       const Place pl = line.at(a, pos, lane);
-      x.v = seq_view_of(a, pl.seq, lane == 0 && warp == kCopyWarp);
+      x.v = seq_view(a, pl.seq);
       x.seq = pl.seq;
       x.head = pl.unit / pl.row_tiles;
       x.row0 = (pl.unit - x.head * pl.row_tiles) * a.tile_rows;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
   };
   long long ahead = 0;
   if (warp == kCopyWarp) {
-    const Line line(a, lane);
+    const Line line(a, lane, blockIdx.x == 0);
     const long long stretch = line.stretch(a, gridDim.x);
     pos_end = min(line.total, (blockIdx.x + 1) * stretch);
     ahead = look_ahead(line, blockIdx.x * stretch, st.seg[0]);
