@@ -453,9 +453,10 @@ int nq_cache_read(const nq_kv_cache* cache, const int32_t* slots, int64_t tokens
  * Few rows (up to 16; see the library's choice at its place): a probability
  * times a value group's scale is held as two bf16 (2^-17).  More rows:
  * probabilities, and values relative to a power of two of their key, are
- * rounded to fp16 (2^-11 each), with a floor of 2^-31 of the row's largest
- * probability (value groups of a key 2^-14 and more below its largest lose
- * precision).  The result does not depend on timing (pieces are merged in
+ * rounded to fp16 (2^-11 each); with 2^e_j the power of two at or below key j's
+ * largest value scale (e_j = -24 for a key of zero values), the products p_j 2^e_j
+ * have a floor of 2^-31 of the row's largest, and value groups of a key 2^-14 and
+ * more below its largest lose precision.  The result does not depend on timing (pieces are merged in
  * order).
  * workspace: device scratch of nq_tree_attention_workspace_bytes(...) for the
  * same arguments or for more sequences and drafted tokens in all (seqs, total),

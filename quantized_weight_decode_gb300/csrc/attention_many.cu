@@ -17,10 +17,11 @@
 // below the block's largest (off by 2^-33 of that); values are code times the
 // group's scale over a power of two 2^e of the key (one rounding, 2^-11 at
 // most), and 2^e goes into the probability, which is rounded once (2^-11 of
-// itself, 2^-25 at least).  The probabilities' reference is kept so that the
-// largest lies in 2^6 .. 2^14: it moves only when one passes 2^14 (then sums and
-// O are scaled), so the fp16 floor is 2^-31 and less of the largest.  Sums of
-// probabilities are fp32, of the unrounded ones.
+// itself, 2^-25 at least).  The reference is kept so that the largest such product
+// lies in 2^6 .. 2^14: it moves only when one passes 2^14 (then sums and O are
+// scaled), so the fp16 floor is 2^-31 and less of the largest.  A key whose values
+// are all zero has e = -24, below any other key's: however probable, it does not raise
+// the floor.  Sums of probabilities are fp32, of the unrounded ones.
 //
 // Warps have roles, joined by barriers in shared memory alone: one copies the
 // codes and scales of tiles of 128 keys (two pages, bulk copies into rings),
@@ -456,7 +457,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
             }
             most = fmaxf(most, fabsf(sv[g]));
           }
-          const unsigned e = most == 0.f ? 0x3F800000u : __float_as_uint(most) & 0x7F800000u;
+          // (without values: the smallest power of FP16, so that the key's probability,
+          // which gives nothing to O, leaves the reference to the keys that do)
+          const unsigned e = most == 0.f ? 0x33800000u : __float_as_uint(most) & 0x7F800000u;
           st.log2_e[slot][key] = ok ? static_cast<float>(static_cast<int>(e >> 23) - 127) : -INFINITY;
 #pragma unroll
           for (int g = 0; g < G; ++g)
