@@ -159,6 +159,31 @@ def _stream_handle(stream) -> int | None:
     return stream.cuda_stream or None
 
 
+def _stream_object(stream):
+    """torch's object of a stream given as None (the current one), a handle or an object."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for a call's result or scratch.  For a call on another stream than the
+    current one it is taken for that stream (a piece that the current stream's
+    pending work still uses would be written too early), and it is not handed out
+    again before what the current stream has read of it by its release."""
+    import torch
+    if stream is None or _stream_handle(stream) == _current_stream_handle():
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(_stream_object(stream)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _dptr(t):
     return None if t is None else int(t.data_ptr())
 
@@ -510,7 +535,7 @@ def rope(x, positions, steps, out=None, layout: int = ROPE_HALF, factor: float =
     xs = _heads_last(x, "rope")
     tokens, heads, dim = x.shape
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+        out = _empty((tokens, heads, dim), x.dtype, x.device, stream)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("rope: out has another shape or type than x")
     os = _heads_last(out, "rope")
@@ -534,12 +559,13 @@ class _CacheStruct(ctypes.Structure):
 class AttentionPlan:
     """What calls of KVCache.attention over batches of one size share: the
     bounds it was made for, the workspace, and the outputs of calls that bring
-    none of their own (torch memory, kept by the plan).  Calls sharing a plan
-    must be ordered (one stream), and each overwrites the outputs of the one
-    before."""
+    none of their own (torch memory, kept by the plan, and beyond it until the
+    streams of its calls are done with it).  Calls sharing a plan must be ordered
+    (one stream), and each overwrites the outputs of the one before.  `stream`:
+    the stream of its calls, if that is not the current one."""
 
     def __init__(self, seqs: int, max_drafts: int, q_heads: int, kv_heads: int, head_dim: int,
-                 max_context: int, device="cuda"):
+                 max_context: int, device="cuda", stream=None):
         import torch
         v = ctypes.c_size_t()
         _check(lib().nq_tree_attention_workspace_bytes(seqs, max_drafts, seqs * max_drafts, q_heads,
@@ -548,19 +574,29 @@ class AttentionPlan:
                "nq_tree_attention_workspace_bytes")
         self.seqs, self.max_drafts, self.max_context = seqs, max_drafts, max_context
         self.bytes = int(v.value)
-        self.workspace = torch.empty(self.bytes, dtype=torch.uint8, device=device) if self.bytes else None
+        self.workspace = _empty(self.bytes, torch.uint8, device, stream) if self.bytes else None
         self._workspace_ptr = _dptr(self.workspace)
         self._outputs = {}
+        self._home = _stream_handle(stream) if self.bytes else None  # the stream that the workspace was taken for
 
-    def outputs(self, total: int, q_heads: int, head_dim: int, device):
-        """The plan's (out, lse) for `total` drafted tokens."""
+    def outputs(self, total: int, q_heads: int, head_dim: int, device, stream=None):
+        """The plan's (out, lse) for `total` drafted tokens, for a call on `stream`."""
+        import torch
+        handle = _stream_handle(stream)
         got = self._outputs.get((total, q_heads, head_dim))
         if got is None:
-            import torch
-            got = (torch.empty((total, q_heads, head_dim), dtype=torch.bfloat16, device=device),
-                   torch.empty((total, q_heads), dtype=torch.float32, device=device))
+            got = (_empty((total, q_heads, head_dim), torch.bfloat16, device, stream),
+                   _empty((total, q_heads), torch.float32, device, stream), handle)
             self._outputs[(total, q_heads, head_dim)] = got
-        return got
+        elif got[2] != handle:
+            for t in got[:2]:
+                t.record_stream(_stream_object(stream))
+        return got[:2]
+
+    def _on(self, stream, handle):
+        """Keeps the workspace until a call on `stream` is done with it."""
+        if self.workspace is not None and self._home != handle:
+            self.workspace.record_stream(_stream_object(stream))
 
 
 class KVCache:
@@ -622,7 +658,7 @@ class KVCache:
             if q.shape != (tokens, heads, self.head_dim) or q.dtype != dtype:
                 raise ValueError("append: q of another shape or type than k")
             if q_out is None:
-                q_out = torch.empty((tokens, heads, self.head_dim), dtype=torch.bfloat16, device=q.device)
+                q_out = _empty((tokens, heads, self.head_dim), torch.bfloat16, q.device, stream)
             elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
                 raise ValueError("append: q_out of another shape than q, or not bfloat16")
             os = _heads_last(q_out, "append")
@@ -652,9 +688,9 @@ class KVCache:
         dtype = dtype or (torch.bfloat16 if k_out is None else k_out.dtype)
         shape = (n, self.kv_heads, self.head_dim)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=slots.device)
+            k_out = _empty(shape, dtype, slots.device, stream)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=slots.device)
+            v_out = _empty(shape, dtype, slots.device, stream)
         for t in (k_out, v_out):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"read: contiguous outputs of shape {shape} and type {dtype} expected")
@@ -696,9 +732,10 @@ class KVCache:
             _vector(tree, torch.int64, total, "attention: tree")
         if plan is None:
             drafts = min(64, total) if starts is not None else -(-total // seqs)
-            plan = self.attention_plan(seqs, max(1, drafts), heads, width * CACHE_PAGE)
+            plan = AttentionPlan(seqs, max(1, drafts), heads, self.kv_heads, self.head_dim, width * CACHE_PAGE,
+                                 self.k_codes.device, stream)
         if out is None or lse is None:
-            own = plan.outputs(total, heads, dim, q.device)
+            own = plan.outputs(total, heads, dim, q.device, stream)
         if out is None:
             out = own[0]
         elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
@@ -707,12 +744,14 @@ class KVCache:
             lse = own[1]
         else:
             _vector(lse, torch.float32, total * heads, "attention: lse")
+        handle = _stream_handle(stream)
+        plan._on(stream, handle)
         rc = lib().nq_tree_attention(
             self._ref, q.data_ptr(), qs[0], qs[1], total, heads, page_table.data_ptr(),
             page_table.stride(0), width, lengths.data_ptr(), None if starts is None else starts.data_ptr(),
             None if tree is None else tree.data_ptr(), seqs, plan.max_drafts, plan.max_context,
             self.head_dim ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-            plan._workspace_ptr, plan.bytes, _stream_handle(stream))
+            plan._workspace_ptr, plan.bytes, handle)
         if rc:
             _check(rc, "nq_tree_attention")
         return out, lse
