@@ -246,9 +246,9 @@ def pack_device(codes, scales, bits: int, packed=None, scales_packed=None, strea
     N, K = codes.shape
     cb, sb = packed_bytes(K, N, bits)
     if packed is None:
-        packed = torch.empty(cb, dtype=torch.uint8, device=codes.device)
+        packed = _empty(cb, torch.uint8, codes.device, stream)
     if scales_packed is None:
-        scales_packed = torch.empty(sb // 2, dtype=torch.int16, device=codes.device)
+        scales_packed = _empty(sb // 2, torch.int16, codes.device, stream)
     _check(lib().nq_pack_device(_dptr(codes), _dptr(scales), K, N, bits, _dptr(packed),
                                 _dptr(scales_packed), _stream_handle(stream)), "nq_pack_device")
     return packed, scales_packed
@@ -260,9 +260,9 @@ def quantize_rtn(w, bits: int, codes=None, scales=None, stream=None):
     import torch
     N, K = w.shape
     if codes is None:
-        codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
+        codes = _empty((N, K), torch.int8, w.device, stream)
     if scales is None:
-        scales = torch.empty((N, K // 64), dtype=torch.int16, device=w.device)
+        scales = _empty((N, K // 64), torch.int16, w.device, stream)
     _check(lib().nq_quantize_rtn(_dptr(w), K, N, bits, _dptr(codes), _dptr(scales),
                                  _stream_handle(stream)), "nq_quantize_rtn")
     return codes, scales
@@ -274,9 +274,9 @@ def quantize_search(w, bits: int, imatrix=None, codes=None, scales=None, stream=
     import torch
     N, K = w.shape
     if codes is None:
-        codes = torch.empty((N, K), dtype=torch.int8, device=w.device)
+        codes = _empty((N, K), torch.int8, w.device, stream)
     if scales is None:
-        scales = torch.empty((N, K // 64), dtype=torch.int16, device=w.device)
+        scales = _empty((N, K // 64), torch.int16, w.device, stream)
     _check(lib().nq_quantize_search(_dptr(w), _dptr(imatrix), K, N, bits, _dptr(codes),
                                     _dptr(scales), _stream_handle(stream)), "nq_quantize_search")
     return codes, scales
@@ -352,13 +352,13 @@ def gemv_head(packed, scales, x, K: int, N: int, T: int, bits: int, y=None, work
     import torch
     dev = x.device
     if workspace is None:
-        workspace = torch.empty(head_workspace_bytes(), dtype=torch.uint8, device=dev)
+        workspace = _empty(head_workspace_bytes(), torch.uint8, dev, stream)
     if argmax is None:
-        argmax = torch.empty(T, dtype=torch.int32, device=dev)
+        argmax = _empty(T, torch.int32, dev, stream)
     if maxval is None:
-        maxval = torch.empty(T, dtype=torch.float32, device=dev)
+        maxval = _empty(T, torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = _empty(T, torch.float32, dev, stream)
     _check(lib().nq_gemv_head(_dptr(packed), _dptr(scales), _dptr(x), _dptr(y), K, N, T, bits,
                               _dptr(argmax), _dptr(maxval), _dptr(lse), _dptr(workspace),
                               workspace.numel() * workspace.element_size(),
@@ -383,18 +383,18 @@ def gemv_head_topk(packed, scales, x, K: int, N: int, T: int, bits: int, k: int,
     import torch
     dev = x.device
     if workspace is None:
-        workspace = torch.empty(head_topk_workspace_bytes(), dtype=torch.uint8, device=dev)
+        workspace = _empty(head_topk_workspace_bytes(), torch.uint8, dev, stream)
     kk = max(k, 1)          # a bad k is the library's to reject
     if topk_idx is None:
-        topk_idx = torch.empty((T, kk), dtype=torch.int32, device=dev)
+        topk_idx = _empty((T, kk), torch.int32, dev, stream)
     if topk_val is None:
-        topk_val = torch.empty((T, kk), dtype=torch.float32, device=dev)
+        topk_val = _empty((T, kk), torch.float32, dev, stream)
     if argmax is None:
-        argmax = torch.empty(T, dtype=torch.int32, device=dev)
+        argmax = _empty(T, torch.int32, dev, stream)
     if maxval is None:
-        maxval = torch.empty(T, dtype=torch.float32, device=dev)
+        maxval = _empty(T, torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = _empty(T, torch.float32, dev, stream)
     _check(lib().nq_gemv_head_topk(_dptr(packed), _dptr(scales), _dptr(x), _dptr(y), K, N, T, bits,
                                    k, _dptr(topk_idx), _dptr(topk_val), _dptr(argmax),
                                    _dptr(maxval), _dptr(lse), _dptr(workspace),
@@ -412,11 +412,11 @@ def gemv_head_noalloc(packed, scales, x, K: int, N: int, T: int, bits: int, y=No
     import torch
     dev = x.device
     if argmax is None:
-        argmax = torch.empty(T, dtype=torch.int32, device=dev)
+        argmax = _empty(T, torch.int32, dev, stream)
     if maxval is None:
-        maxval = torch.empty(T, dtype=torch.float32, device=dev)
+        maxval = _empty(T, torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = _empty(T, torch.float32, dev, stream)
     _check(lib().nq_gemv_head_noalloc(_dptr(packed), _dptr(scales), _dptr(x), _dptr(y), K, N, T,
                                       bits, _dptr(argmax), _dptr(maxval), _dptr(lse),
                                       _stream_handle(stream)), "nq_gemv_head_noalloc")
@@ -426,7 +426,7 @@ def gemv_head_noalloc(packed, scales, x, K: int, N: int, T: int, bits: int, y=No
 def dequant(packed, scales, K: int, N: int, bits: int, out=None, stream=None):
     import torch
     if out is None:
-        out = torch.empty((N, K), dtype=torch.float32, device=packed.device)
+        out = _empty((N, K), torch.float32, packed.device, stream)
     _check(lib().nq_dequant(_dptr(packed), _dptr(scales), _dptr(out), K, N, bits,
                             _stream_handle(stream)), "nq_dequant")
     return out
@@ -475,7 +475,7 @@ class QuantizedWeight:
         import torch
         T = x.shape[0]
         if y is None:
-            y = torch.empty((T, self.N), dtype=torch.float32, device=x.device)
+            y = _empty((T, self.N), torch.float32, x.device, stream)
         gemv(self.packed, self.scales, x, y, self.K, self.N, T, self.bits, route, ksplit, stream)
         return y
 

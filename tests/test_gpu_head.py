@@ -255,3 +255,32 @@ def test_head_proposal_head_shape(bits, T):
     codes, sb = oracle_inputs(case, rows)
     y_ref, e_ref = oracle.gemv(codes, sb, case["xb"][:T])
     assert oracle.max_violation(y[:, rows], y_ref, e_ref) <= 1.0
+
+
+@pytest.mark.parametrize("k", [0, 8])
+def test_head_on_another_stream_keeps_its_workspace(k):
+    """A workspace taken by a call on another stream is not handed out before
+    the call has run, nor its results taken from memory still in use."""
+    K, N, T, bits = 1024, 4096, 3, 5
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    qw = nqp.QuantizedWeight.from_fp32(torch.randn((N, K), device="cuda", generator=gen) * 0.03, bits)
+    x = torch.randn((T, K), device="cuda", generator=gen).to(torch.bfloat16)
+    call = lambda **kw: (nqp.gemv_head_topk(qw.packed, qw.scales, x, K, N, T, bits, k, **kw) if k  # noqa: E731
+                         else nqp.gemv_head(qw.packed, qw.scales, x, K, N, T, bits, **kw))
+    size = nqp.head_topk_workspace_bytes() if k else nqp.head_workspace_bytes()
+    want = [t.clone() for t in call()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)                    # some 20 ms
+    got = call(stream=s)
+    junk = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda._sleep(40_000_000)
+    junk += [torch.full_like(t, -7) for t in want for _ in range(4)]
+    del junk                                             # released while the fills are pending
+    got = call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert nqp.last_device_error() == 0
