@@ -667,8 +667,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             unpack2(add2(z[i], pack2(r[2 * i], r[2 * i + 1])), y[0][2 * i], y[0][2 * i + 1]);
-          if (masked && draft >= 0 && key0 + kt < key_end) {
-            const unsigned seen = st.rows[draft][c >> 2] >> (8 * (c & 3));
+          // (a key that is none for every row too: e = -inf does not hide it from a query of NaN)
+          if ((masked && draft >= 0) || log2_e == -INFINITY) {
+            const unsigned seen = log2_e == -INFINITY ? 0u : st.rows[draft][c >> 2] >> (8 * (c & 3));
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (!(seen >> i & 1u)) y[0][i] = -INFINITY;
