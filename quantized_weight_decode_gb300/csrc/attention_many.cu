@@ -13,8 +13,8 @@
 // times its scale in fp32, and no reduction over the rows is needed.
 //
 // Everything is fp16 on the tensor cores: codes are exact; queries are bf16
-// values times one power of two for the block, exact but for values 2^-22
-// below the block's largest (off by 2^-33 of that); values are code times the
+// values times a power of two a row, exact but for values 2^-22 below the row's
+// largest (off by 2^-33 of that); values are code times the
 // group's scale over a power of two 2^e of the key (one rounding, 2^-11 at
 // most), and 2^e goes into the probability, which is rounded once (2^-11 of
 // itself, 2^-25 at least).  The reference is kept so that the largest such product
@@ -71,6 +71,7 @@ struct Segment {     // a unit's tiles that a block takes in one go
 template <int G>
 struct SmallMem {
   alignas(16) float ref[128];            // minus the rows' references (0 before the first); read 16 bytes at a time
+  alignas(16) float undo[128];           // one over the rows' powers of two
   alignas(16) float k[kScaleSlots][kTileKeys][G < 4 ? 2 : 4];     // key groups' scales times the logits' factor
   alignas(16) uint16_t raw[kScaleSlots][2][kTileKeys * G];        // FP16 scales as the cache has them
   alignas(8) uint16_t ratio[kScaleSlots][kTileKeys][G < 4 ? 2 : 4];  // fp16 scales of the value groups over 2^e
@@ -84,7 +85,6 @@ struct SmallMem {
   float sum[4][128];
   int id[128];               // row of q, out and lse
   unsigned char set[128];    // rows with a reference
-  unsigned most_q;
   uint32_t tmem;
   int abort;
   Segment seg[2];
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
   using C = Many<D, KB, VB>;
   constexpr int G = C::G, NH = C::NH, GP = C::GP;
   using Small = SmallMem<G>;
-  static_assert(offsetof(Small, ref) % 16 == 0 && offsetof(Small, k) % 16 == 0 && offsetof(Small, raw) % 16 == 0 &&
+  static_assert(offsetof(Small, ref) % 16 == 0 && offsetof(Small, undo) % 16 == 0 && offsetof(Small, k) % 16 == 0 && offsetof(Small, raw) % 16 == 0 &&
                     offsetof(Small, ratio) % 8 == 0 && offsetof(Small, kraw_full) % 8 == 0,
                 "wide accesses and copies");
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -561,14 +561,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
       }
       if (tid < 16) st.poison[tid >> 2][tid & 3] = 0u;
       if (tid < 128) st.set[tid] = 0;
-      if (tid == 0) st.most_q = 0u;
-      softmax_sync<C::kSoftmaxThreads>();
-      // Queries: runs of 8 channels, scaled by one power of two.
-      float undo;
+      // Queries: runs of 8 channels, each row scaled by a power of two of its own
+      // (one for all rows would let a row of huge values take the others' precision).
       {
         constexpr int kRuns = D / 8, kItems = C::kMaxRows * kRuns / C::kSoftmaxThreads;
+        static_assert(kRuns <= 32 && C::kSoftmaxThreads % kRuns == 0, "a row's runs lie side by side in a warp");
         uint4 raw[kItems];
-        unsigned most = 0u;
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
           const int e = tid + i * C::kSoftmaxThreads, n = e / kRuns, c = e % kRuns;
@@ -581,27 +579,22 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
         }
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
+          const int e = tid + i * C::kSoftmaxThreads, n = e / kRuns, c = e % kRuns;
           const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          unsigned most = 0u;  // the row's largest finite magnitude
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const unsigned lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
             if (lo < 0x7F80u) most = max(most, lo);
             if (hi < 0x7F80u) most = max(most, hi);
           }
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0 && most) atomicMax(&st.most_q, most);
-        softmax_sync<C::kSoftmaxThreads>();
-        // largest magnitude into [2^7, 2^8): exponent field of a bf16
-        const int field = static_cast<int>(st.most_q >> 7);
-        const int ex = st.most_q == 0u ? 0 : max(-120, min(120, 134 - field));
-        const float up = __int_as_float((ex + 127) << 23);
-        undo = __int_as_float((127 - ex) << 23);
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          const int e = tid + i * C::kSoftmaxThreads, n = e / kRuns, c = e % kRuns;
+          for (int k = kRuns / 2; k >= 1; k >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
+          // into [2^7, 2^8): exponent field of a bf16
+          const int ex = most == 0u ? 0 : max(-120, min(120, 134 - static_cast<int>(most >> 7)));
+          const float up = __int_as_float((ex + 127) << 23);
+          if (c == 0) st.undo[n] = __int_as_float((127 - ex) << 23);
           if (n < npad) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
             float f[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -618,6 +611,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
         }
         fence_proxy_async_smem();
       }
+      softmax_sync<C::kSoftmaxThreads>();
       queries_done<C::kSoftmaxThreads>();
 
       bool unset = false;  // this lane's row (below) has no reference after the tiles so far
@@ -629,10 +623,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
           const float4 x = *reinterpret_cast<const float4*>(st.k[slot][kt]);
           const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int g = 0; g < G; ++g) kk[g] = pack2(f[g] * undo, f[g] * undo);
+          for (int g = 0; g < G; ++g) kk[g] = pack2(f[g], f[g]);
         } else {
 #pragma unroll
-          for (int g = 0; g < G; ++g) kk[g] = pack2(st.k[slot][kt][g] * undo, st.k[slot][kt][g] * undo);
+          for (int g = 0; g < G; ++g) kk[g] = pack2(st.k[slot][kt][g], st.k[slot][kt][g]);
         }
         const float log2_e = st.log2_e[slot][kt];
         const float inv_e = log2_e == -INFINITY ? 0.f : __int_as_float((127 - static_cast<int>(log2_e)) << 23);
@@ -649,7 +643,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
           float y[GL][8];
           unsigned long long z[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = e2;
+          for (int i = 0; i < 4; ++i) z[i] = 0ull;
 #pragma unroll
           for (int g0 = 0; g0 < G; g0 += GL) {
 #pragma unroll
@@ -661,12 +655,13 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
 #pragma unroll
               for (int i = 0; i < 4; ++i) z[i] = fma2(pack2(y[g][2 * i], y[g][2 * i + 1]), kk[g0 + g], z[i]);
           }
-          const float4 r0 = *reinterpret_cast<const float4*>(st.ref + 8 * c);
-          const float4 r1 = *reinterpret_cast<const float4*>(st.ref + 8 * c + 4);
-          const float r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            unpack2(add2(z[i], pack2(r[2 * i], r[2 * i + 1])), y[0][2 * i], y[0][2 * i + 1]);
+          for (int i = 0; i < 2; ++i) {
+            const float4 u = *reinterpret_cast<const float4*>(st.undo + 8 * c + 4 * i);
+            const float4 r = *reinterpret_cast<const float4*>(st.ref + 8 * c + 4 * i);
+            unpack2(add2(fma2(z[2 * i], pack2(u.x, u.y), e2), pack2(r.x, r.y)), y[0][4 * i], y[0][4 * i + 1]);
+            unpack2(add2(fma2(z[2 * i + 1], pack2(u.z, u.w), e2), pack2(r.z, r.w)), y[0][4 * i + 2], y[0][4 * i + 3]);
+          }
           // (a key that is none for every row too: e = -inf does not hide it from a query of NaN)
           if ((masked && draft >= 0) || log2_e == -INFINITY) {
             const unsigned seen = log2_e == -INFINITY ? 0u : st.rows[draft][c >> 2] >> (8 * (c & 3));
