@@ -438,7 +438,8 @@ int nq_cache_read(const nq_kv_cache* cache, const int32_t* slots, int64_t tokens
  * lengths[s] + i.  Position p of s lies in page page_table[s][p / 64], offset
  * p % 64.  Query head h reads kv head h / (q_heads / kv_heads).
  *   q: bf16 [total, q_heads, head_dim], strides in elements (multiples of 8);
- *   page_table: int32 [seqs][table_width], row stride table_stride;
+ *   page_table: int32 [seqs][table_width], row stride table_stride, table_width
+ *   <= (2^31 - 256) / 64;
  *   lengths: int32 [seqs]; starts: int32 [seqs + 1], the first drafted token
  *   of each sequence and the total, or NULL: total / seqs each;
  *   tree: [total] masks, or NULL: a chain (bits 0 .. i);

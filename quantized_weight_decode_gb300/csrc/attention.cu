@@ -632,7 +632,8 @@ int nq_tree_attention(const nq_kv_cache* cache, const void* q, int64_t q_token_s
   if (int rc = check_attention(seqs, max_drafts, q_heads, cache->kv_heads, cache->head_dim, total,
                                max_context))
     return rc;
-  if (table_width < 0 || table_width > INT_MAX / kPage) return NQ_EINVAL;
+  // (a sequence's keys rounded up to whole tiles stay within an int)
+  if (table_width < 0 || table_width > (INT_MAX - 255) / kPage) return NQ_EINVAL;
   if (!starts && total % seqs) return NQ_EINVAL;
   if (!starts && total / seqs > max_drafts) return NQ_EINVAL;
   if (total == 0) return NQ_OK;

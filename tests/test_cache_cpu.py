@@ -215,3 +215,12 @@ def test_binding_refuses_wrong_tensors():
         nqp.rope(k, s, torch.zeros(32, dtype=torch.int64), out=k.double())
     with pytest.raises(ValueError):
         nqp.rope(k.transpose(1, 2), s, torch.zeros(32, dtype=torch.int64))
+
+
+def test_attention_refuses_tables_whose_keys_pass_an_int():
+    """Keys are counted in whole tiles of up to 128 in 32-bit integers: a table of
+    2^31 - 64 keys would have passed them."""
+    most = ((1 << 31) - 256) // 64
+    assert most * 64 + 127 < 1 << 31 <= (most + 3) * 64 + 127
+    for width in (most + 1, (1 << 31) // 64 - 1, (1 << 31) - 1):
+        assert _attention(width=width, stride=width) == nqp.EINVAL
