@@ -510,6 +510,13 @@ def _vector(t, dtype, n: int, where: str):
     return t
 
 
+def _reachable(dev: int, where: str, *tensors) -> None:
+    """Refuses tensors (None: not given) that are not in the memory of cuda device `dev`."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError(f"{where}: cuda tensors on one device expected")
+
+
 def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", scale_factor: float = 1.0,
                trained_context: float = 0.0, device="cuda"):
     """Rotary steps (nq_rope_steps): (int64 tensor [rotary_dim / 2] on `device`,
@@ -542,7 +549,9 @@ def rope(x, positions, steps, out=None, layout: int = ROPE_HALF, factor: float =
     _vector(positions, torch.int32, tokens, "rope: positions")
     half = steps.numel()
     _vector(steps, torch.int64, half, "rope: steps")
-    rc = lib().nq_rope(x.data_ptr(), out.data_ptr(), _dtype_code(x), tokens, heads, dim, 2 * half,
+    code = _dtype_code(x)
+    _reachable(x.get_device(), "rope", out, positions, steps)
+    rc = lib().nq_rope(x.data_ptr(), out.data_ptr(), code, tokens, heads, dim, 2 * half,
                        xs[0], xs[1], os[0], os[1], positions.data_ptr(), steps.data_ptr(), layout,
                        factor, adjoint, _stream_handle(stream))
     if rc:
@@ -577,26 +586,22 @@ class AttentionPlan:
         self.workspace = _empty(self.bytes, torch.uint8, device, stream) if self.bytes else None
         self._workspace_ptr = _dptr(self.workspace)
         self._outputs = {}
-        self._home = _stream_handle(stream) if self.bytes else None  # the stream that the workspace was taken for
+        # the stream that the workspace was taken for
+        self._home = _stream_handle(stream) if self.bytes else None
 
     def outputs(self, total: int, q_heads: int, head_dim: int, device, stream=None):
         """The plan's (out, lse) for `total` drafted tokens, for a call on `stream`."""
-        import torch
-        handle = _stream_handle(stream)
         got = self._outputs.get((total, q_heads, head_dim))
+        handle = _stream_handle(stream)
         if got is None:
+            import torch
             got = (_empty((total, q_heads, head_dim), torch.bfloat16, device, stream),
                    _empty((total, q_heads), torch.float32, device, stream), handle)
             self._outputs[(total, q_heads, head_dim)] = got
         elif got[2] != handle:
             for t in got[:2]:
                 t.record_stream(_stream_object(stream))
-        return got[:2]
-
-    def _on(self, stream, handle):
-        """Keeps the workspace until a call on `stream` is done with it."""
-        if self.workspace is not None and self._home != handle:
-            self.workspace.record_stream(_stream_object(stream))
+        return got
 
 
 class KVCache:
@@ -616,10 +621,13 @@ class KVCache:
                     or not s.is_contiguous() or tuple(s.shape) != (pages, heads, CACHE_PAGE, groups)
                     or tuple(c.shape) != (pages, heads, CACHE_PAGE, self.head_dim * bits // 8)):
                 raise ValueError("KVCache: codes or scales of another type, shape or layout than documented")
+        if len({t.device for t in (k_codes, k_scales, v_codes, v_scales)}) != 1:
+            raise ValueError("KVCache: codes and scales on one device expected")
         self._struct = _CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                     v_scales.data_ptr(), pages, heads, self.head_dim, self.k_bits,
                                     self.v_bits)
         self._ref = ctypes.addressof(self._struct)
+        self._device = k_codes.get_device()
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, k_bits: int = 8, v_bits: int = 8,
@@ -671,7 +679,9 @@ class KVCache:
             half = steps.numel()
             _vector(steps, torch.int64, half, "append: steps")
             pos_ptr, steps_ptr = positions.data_ptr(), steps.data_ptr()
-        rc = lib().nq_cache_append(self._ref, k.data_ptr(), v.data_ptr(), _dtype_code(k), tokens, ks[0],
+        code = _dtype_code(k)
+        _reachable(self._device, "append", k, v, slots, q, q_out, None if steps is None else positions, steps)
+        rc = lib().nq_cache_append(self._ref, k.data_ptr(), v.data_ptr(), code, tokens, ks[0],
                                    ks[1], vs[0], vs[1], slots.data_ptr(), q_ptr, out_ptr, heads, qs[0],
                                    qs[1], os[0], os[1], pos_ptr, steps_ptr, 2 * half, layout, factor,
                                    _stream_handle(stream))
@@ -694,8 +704,10 @@ class KVCache:
         for t in (k_out, v_out):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"read: contiguous outputs of shape {shape} and type {dtype} expected")
+        code = _dtype_code(k_out)
+        _reachable(self._device, "read", slots, k_out, v_out)
         rc = lib().nq_cache_read(self._ref, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
-                                 _dtype_code(k_out), _stream_handle(stream))
+                                 code, _stream_handle(stream))
         if rc:
             _check(rc, "nq_cache_read")
         return k_out, v_out
@@ -730,6 +742,7 @@ class KVCache:
             _vector(starts, torch.int32, seqs + 1, "attention: starts")
         if tree is not None:
             _vector(tree, torch.int64, total, "attention: tree")
+        _reachable(self._device, "attention", q, page_table, lengths, starts, tree, out, lse)
         if plan is None:
             drafts = min(64, total) if starts is not None else -(-total // seqs)
             plan = AttentionPlan(seqs, max(1, drafts), heads, self.kv_heads, self.head_dim, width * CACHE_PAGE,
@@ -745,7 +758,8 @@ class KVCache:
         else:
             _vector(lse, torch.float32, total * heads, "attention: lse")
         handle = _stream_handle(stream)
-        plan._on(stream, handle)
+        if plan._home != handle and plan.bytes:              # keep the workspace until the call is done with it
+            plan.workspace.record_stream(_stream_object(stream))
         rc = lib().nq_tree_attention(
             self._ref, q.data_ptr(), qs[0], qs[1], total, heads, page_table.data_ptr(),
             page_table.stride(0), width, lengths.data_ptr(), None if starts is None else starts.data_ptr(),

@@ -224,3 +224,21 @@ def test_attention_refuses_tables_whose_keys_pass_an_int():
     assert most * 64 + 127 < 1 << 31 <= (most + 3) * 64 + 127
     for width in (most + 1, (1 << 31) // 64 - 1, (1 << 31) - 1):
         assert _attention(width=width, stride=width) == nqp.EINVAL
+
+
+def test_binding_refuses_tensors_that_the_kernels_cannot_reach():
+    """Host memory, or memory of another device than the cache's."""
+    import torch
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    x, steps = torch.zeros((3, 2, 64), dtype=torch.bfloat16), torch.zeros(32, dtype=torch.int64)
+    c = nqp.KVCache.empty(2, 2, 64, device="cpu")
+    far = nqp.KVCache.empty(2, 2, 64, device="meta")
+    calls = [lambda: nqp.rope(x, i(3), steps), lambda: nqp.rope(x.to("meta"), i(3), steps), lambda: c.append(x, x, i(3)),
+             lambda: c.append(x, x, i(3), q=x, positions=i(3), steps=steps), lambda: far.append(x, x, i(3)),
+             lambda: c.read(i(3)), lambda: c.attention(x, i(1, 1), i(1)), lambda: c.attention(x, i(1, 1).to("meta"), i(1))]
+    for k, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {k}")
+    with pytest.raises(ValueError):
+        nqp.KVCache(c.k_codes, c.k_scales, far.v_codes, far.v_scales)
