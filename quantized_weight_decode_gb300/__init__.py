@@ -743,12 +743,17 @@ class KVCache:
         if tree is not None:
             _vector(tree, torch.int64, total, "attention: tree")
         _reachable(self._device, "attention", q, page_table, lengths, starts, tree, out, lse)
-        if plan is None:
+        if seqs == 0:                        # an empty batch: nothing to launch
+            if total:
+                raise ValueError("attention: drafted tokens of no sequence")
+            plan = None
+        elif plan is None:
             drafts = min(64, total) if starts is not None else -(-total // seqs)
             plan = AttentionPlan(seqs, max(1, drafts), heads, self.kv_heads, self.head_dim, width * CACHE_PAGE,
                                  self.k_codes.device, stream)
         if out is None or lse is None:
-            own = plan.outputs(total, heads, dim, q.device, stream)
+            own = (plan.outputs(total, heads, dim, q.device, stream) if plan is not None
+                   else (torch.empty_like(q), torch.empty((0, heads), dtype=torch.float32, device=q.device)))
         if out is None:
             out = own[0]
         elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
@@ -757,6 +762,8 @@ class KVCache:
             lse = own[1]
         else:
             _vector(lse, torch.float32, total * heads, "attention: lse")
+        if plan is None:
+            return out, lse
         handle = _stream_handle(stream)
         if plan._home != handle and plan.bytes:              # keep the workspace until the call is done with it
             plan.workspace.record_stream(_stream_object(stream))
