@@ -591,8 +591,6 @@ int check_attention(int seqs, int max_drafts, int q_heads, int kv_heads, int dim
   if (kv_heads < 1 || q_heads < kv_heads || q_heads % kv_heads || q_heads > 65535) return NQ_EINVAL;
   if (total < 0 || total > static_cast<int64_t>(seqs) * max_drafts) return NQ_EINVAL;
   if (max_context < 0 || max_context > INT_MAX - kMaxDrafts) return NQ_EINVAL;
-  if (static_cast<int64_t>(kv_heads) * ((max_drafts * (q_heads / kv_heads) + 7) / 8) > 65535)
-    return NQ_EINVAL;
   return NQ_OK;
 }
 
