@@ -12,6 +12,7 @@ Names follow the C ABI: ``gemv`` is ``nq_gemv``, ``pack`` is ``nq_pack`` ...
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -532,13 +533,42 @@ def rope_steps(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", s
     return torch.from_numpy(steps.view(np.int64)).to(device), factor.value
 
 
+@functools.cache
+def _rope_function():
+    """rope as a function of torch's autograd: linear in x, its gradient is the adjoint."""
+    import torch
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, steps, layout, factor, adjoint, stream):
+            ctx.save_for_backward(positions, steps)
+            ctx.how = layout, factor, adjoint
+            return rope(x.detach(), positions, steps, None, layout, factor, adjoint, stream)
+
+        @staticmethod
+        def backward(ctx, grad):
+            positions, steps = ctx.saved_tensors
+            layout, factor, adjoint = ctx.how
+            if grad.data_ptr() % 16 or (grad.stride(2) != 1 and grad.shape[2] > 1):
+                grad = grad.clone(memory_format=torch.contiguous_format)  # (a sum's gradient is one value with strides of 0)
+            return (rope(grad, positions, steps, None, layout, factor, not adjoint),) + (None,) * 6
+
+    return Rope
+
+
 def rope(x, positions, steps, out=None, layout: int = ROPE_HALF, factor: float = 1.0,
          adjoint: bool = False, stream=None):
     """Rotated x [tokens, heads, head_dim] (fp32 or bf16 cuda; strides allowed in
     the first two dimensions): nq_rope.  positions: int32 [tokens]; steps: int64
     [rotary_dim / 2] (rope_steps).  adjoint: the transposed rotation, which
-    takes the gradient of the result to that of x.  out may be x."""
+    takes the gradient of the result to that of x.  out may be x.  Where x
+    requires a gradient (and gradients are on), so does the result, whose
+    gradient is rotated back by the adjoint; out cannot be given then."""
     import torch
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("rope: no out for a tensor that requires a gradient")
+        return _rope_function().apply(x, positions, steps, layout, factor, adjoint, stream)
     xs = _heads_last(x, "rope")
     tokens, heads, dim = x.shape
     if out is None:

@@ -307,3 +307,45 @@ def test_outputs_on_sixteen_byte_boundaries(dtype):
     assert torch.equal(q_out, kk.to(torch.bfloat16))
     c.append(k.to(dtype), k.to(dtype), slots)
     assert torch.equal(c2.k_codes, c.k_codes) and torch.equal(c2.v_codes, c.v_codes)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rope_in_a_graph_of_gradients(dtype, inter):
+    """A result of a tensor that requires a gradient carries one: the adjoint's,
+    bit for bit, for whatever layout the incoming gradient has, and its own
+    gradient is the rotation again."""
+    steps, factor, _ = _steps(48, scaling="yarn", f=2.0, ctx=4096.0)
+    gen = torch.Generator(device=DEV).manual_seed(19)
+    x, g = (torch.randn((5, 2, 64), device=DEV, generator=gen).to(dtype) for _ in range(2))
+    pos = torch.tensor([7, 123456, -3, 0, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    kw = dict(layout=int(inter), factor=factor)
+    want = nqp.rope(x, pos, steps, **kw)
+    assert not want.requires_grad
+    x.requires_grad_(True)
+    for adjoint in (False, True):
+        back = nqp.rope(g, pos, steps, adjoint=not adjoint, **kw)
+        y = nqp.rope(x, pos, steps, adjoint=adjoint, **kw)
+        assert y.requires_grad and (adjoint or torch.equal(y, want))
+        gx, = torch.autograd.grad(y, x, g)
+        assert gx.dtype == dtype and torch.equal(gx, back)
+    y = nqp.rope(x, pos, steps, **kw)
+    ones = nqp.rope(torch.ones_like(g), pos, steps, adjoint=True, **kw)
+    assert torch.equal(torch.autograd.grad(y.sum(), x, retain_graph=True)[0], ones)      # one value, strides of 0
+    wide = torch.zeros((5, 64, 2), dtype=dtype, device=DEV).transpose(1, 2)              # head_dim not contiguous
+    wide.copy_(g)
+    assert torch.equal(torch.autograd.grad(y, x, wide, retain_graph=True)[0], nqp.rope(g, pos, steps, adjoint=True, **kw))
+    off = torch.zeros(5 * 2 * 64 + 1, dtype=dtype, device=DEV)[1:].view(5, 2, 64)        # off a 16-byte boundary
+    off.copy_(g)
+    assert torch.equal(torch.autograd.grad(y, x, off, retain_graph=True)[0], nqp.rope(g, pos, steps, adjoint=True, **kw))
+    g.requires_grad_(True)
+    gx, = torch.autograd.grad(y, x, g, create_graph=True)
+    assert torch.equal(torch.autograd.grad(gx, g, x.detach())[0], want)
+    with torch.no_grad():
+        assert not nqp.rope(x, pos, steps, **kw).requires_grad
+        z = x.detach().clone().requires_grad_(True)
+        assert nqp.rope(z, pos, steps, out=z, **kw) is z and torch.equal(z, want)
+    for out in (torch.empty_like(want), x):
+        with pytest.raises(ValueError):
+            nqp.rope(x, pos, steps, out=out, **kw)
+    assert nqp.last_device_error() == 0
