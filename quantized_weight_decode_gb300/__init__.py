@@ -625,10 +625,17 @@ class AttentionPlan:
         handle = _stream_handle(stream)
         if got is None:
             import torch
-            got = (_empty((total, q_heads, head_dim), torch.bfloat16, device, stream),
-                   _empty((total, q_heads), torch.float32, device, stream), handle)
+            # one piece for the largest batch, of which every other one takes the
+            # front: it stays where it is (a captured graph may hold it)
+            most = max(total, self.seqs * self.max_drafts)
+            got = self._outputs.get((most, q_heads, head_dim))
+            if got is None:
+                got = (_empty((most, q_heads, head_dim), torch.bfloat16, device, stream),
+                       _empty((most, q_heads), torch.float32, device, stream), handle)
+                self._outputs[(most, q_heads, head_dim)] = got
+            got = got[0][:total], got[1][:total], got[2]
             self._outputs[(total, q_heads, head_dim)] = got
-        elif got[2] != handle:
+        if got[2] != handle:
             for t in got[:2]:
                 t.record_stream(_stream_object(stream))
         return got
