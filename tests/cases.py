@@ -7,6 +7,7 @@ import numpy as np
 
 import oracle
 import synth
+from oracle import cache as oracle_cache
 
 
 def rtn_case(tag, bits, N, K, T, outlier_frac=0.0, seed=0):
@@ -82,3 +83,31 @@ def head_check_self(y, am, mx, lse):
     assert np.array_equal(mx.view(np.uint32), y[np.arange(T), am].view(np.uint32))
     ref = lse64(y)
     assert np.all(np.abs(lse - ref) <= LSE_ABS + LSE_REL * np.abs(ref)), (lse, ref)
+
+
+# ---- attention of drafted tokens
+def attention_products_bar(many, q, k, v, scale, seen):
+    """Bars of one sequence's attention (arguments of the oracle's) that see the
+    products' own precision: (exact outputs, largest error, root of the mean square
+    error).  Few rows: a probability times a scale as two bf16 (2^-17); many:
+    probabilities and values as fp16 (2^-11 each); outputs are rounded to bf16 (2^-8).
+    Largest: these as they stand, of A = sum p |v|, with 2^-16 for sums in fp32;
+    d: what the logits' errors do to a probability.  Mean square: a rounding is
+    spread over its interval, so its square is a third of the largest on average
+    and errors of different keys add as squares, of B^2 = sum (p v)^2: 2^-11 B covers
+    the two of many rows (2^-11 sqrt(2 / 3))."""
+    o, _, spread, mag = oracle_cache.attention(q, k, v, scale, seen)
+    dim, group = q.shape[2], q.shape[1] // k.shape[1]
+    d = 2 * ((dim + 8) * 2.0 ** -24 * mag + 2.0 ** -21)[..., None]
+    u = 2.0 ** -10 if many else 2.0 ** -17
+    b2 = np.zeros_like(o)
+    for t in range(q.shape[0]):
+        js = np.nonzero(seen[t])[0]
+        for h in range(q.shape[1]):
+            x = k[js, h // group] @ q[t, h] * scale
+            p = np.exp(x - x.max())
+            b2[t, h] = (p / p.sum()) ** 2 @ v[js, h // group] ** 2
+    most = 2.0 ** -8 * np.abs(o) + (u + 2.0 ** -16 + d) * spread * (1 + 2.0 ** -8)
+    rms = (np.sqrt(np.mean((2.0 ** -8 * o) ** 2) / 3) + (2.0 ** -11 if many else 2.0 ** -17) * np.sqrt(np.mean(b2))
+           + np.sqrt(np.mean((d * spread) ** 2)))
+    return o, most, rms

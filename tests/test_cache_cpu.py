@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 import quantized_weight_decode_gb300 as nqp
+from cases import attention_products_bar
 from oracle import cache as oc
 
 
@@ -242,3 +243,34 @@ def test_binding_refuses_tensors_that_the_kernels_cannot_reach():
             pytest.fail(f"call {k}")
     with pytest.raises(ValueError):
         nqp.KVCache(c.k_codes, c.k_scales, far.v_codes, far.v_scales)
+
+
+@pytest.mark.parametrize("length", [60, 900])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_the_bars_of_the_attention_see_a_lost_half(length, dim):
+    """Outputs that cancel, with the probabilities rounded in numpy: the formats of
+    the kernels pass, one bf16 alone does not."""
+    def bf16(x):
+        b = np.ascontiguousarray(x, dtype=np.float32).view(np.uint32)
+        return ((b + ((b >> 16 & 1) + 0x7FFF)) & 0xFFFF0000).astype(np.uint32).view(np.float32).astype(np.float64)
+    rng = np.random.default_rng(17)
+    hq, hkv, t = 10, 2, length + 2
+    k, v = (oc.values(rng.integers(-128, 128, (t, hkv, dim)).astype(np.int8),
+                      (rng.uniform(0.3, 2.0, (t, hkv, dim // 64)) / 127).astype(np.float16)) for _ in range(2))
+    v[1::2] = -v[:-1:2]
+    q = bf16(rng.standard_normal((2, hq, dim)) * 2.0 ** -4)
+    seen = np.tril(np.ones((2, t), bool), length)
+    fp16 = lambda x: x.astype(np.float16).astype(np.float64)  # noqa: E731
+    hi_lo = lambda x: bf16(x) + bf16(x - bf16(x))  # noqa: E731
+    for many, good in ((False, hi_lo), (True, fp16)):
+        o, most, rms = attention_products_bar(many, q, k, v, dim ** -0.5, seen)
+        for held, passes in ((good, True), (bf16, False)):
+            got = np.zeros_like(o)
+            for i in range(2):
+                for h in range(hq):
+                    x = np.where(seen[i], k[:, h // 5] @ q[i, h] * dim ** -0.5, -np.inf)
+                    p = np.exp(x - x.max())
+                    vv = fp16(v[:, h // 5]) if many else v[:, h // 5]
+                    got[i, h] = held(p) @ vv / p.sum()
+            err = np.abs(bf16(got) - o)
+            assert (np.all(err <= most) and np.sqrt(np.mean(err ** 2)) <= rms) == passes, (many, passes)
