@@ -86,7 +86,7 @@ struct SmallMem {
   int id[128];               // row of q, out and lse
   unsigned char set[128];    // rows with a reference
   uint32_t tmem;
-  int abort;
+  int abort, lost;           // a wait gave up; one for a copy did
   Segment seg[2];
   // Barriers: copies landed (keys, values, scales) and slots free; scales
   // prepared and free; a half of the fp16 keys, of the values, probabilities
@@ -180,6 +180,15 @@ __device__ __noinline__ void wait_on(uint32_t bar, uint32_t par, int* abort, uns
   const Waiter wt{abort, limit, status};
   (void)wt.wait<false>(bar, par);
 }
+// The same on the barriers of the copies.  A wait that gave up elsewhere does not
+// end it: a slot with a copy under way must not be taken for free, nor its
+// barrier armed again.  All other waits end then, so these are met within their
+// own time (of twice the limit, unless a copy is lost for good).
+__device__ __noinline__ void wait_copy_on(uint32_t bar, uint32_t par, int* lost, int* abort, unsigned long long limit,
+                                          int* status) {
+  const Waiter wt{lost, 2 * limit, status};
+  if (!wt.wait<false>(bar, par)) *const_cast<volatile int*>(abort) = 1;
+}
 
 // Pairs of fp32.
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
@@ -272,7 +281,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
     mbar_init(smem_addr(&st.v_free), 1);
     mbar_init(smem_addr(&st.o_full), 1);
     fence_mbar_init();
-    st.abort = 0;
+    st.abort = st.lost = 0;
   }
   if (D == 64)  // the upper half of O's lanes has no channels: zeros
     for (int e = tid; e < kBlock / 16; e += kThreadsT) st_shared16(sb + C::off_v + kBlock + 16 * e, 0, 0, 0, 0);
@@ -280,6 +289,10 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
   const int pages = a.c.capacity / kPage;
   auto wait = [&](unsigned long long& bar, uint32_t par) {
     if (!mbar_try_wait(smem_addr(&bar), par & 1u)) wait_on(smem_addr(&bar), par & 1u, &st.abort, a.wait_ns, a.status);
+  };
+  auto wait_copy = [&](unsigned long long& bar, uint32_t par) {
+    if (!mbar_try_wait(smem_addr(&bar), par & 1u))
+      wait_copy_on(smem_addr(&bar), par & 1u, &st.lost, &st.abort, a.wait_ns, a.status);
   };
   auto arrive = [&](unsigned long long& bar) {  // one arrival of a warp
     __syncwarp();
@@ -340,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
       auto fill = [&](unsigned long long* full, unsigned long long* free, unsigned slots, uint32_t bytes, unsigned n,
                       const int (&page)[2], auto copy) {
         const unsigned slot = n % slots;
-        if (n >= slots) wait(free[slot], n / slots - 1);
+        if (n >= slots) wait_copy(free[slot], n / slots - 1);
         if (lane == 0) {
           const uint32_t bar = smem_addr(&full[slot]);
           mbar_arrive_expect_tx(bar, bytes * ((page[0] >= 0) + (page[1] >= 0)));
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
       for (int t = 0; t < tiles; ++t) {
         const unsigned n = done + t, slot = n % kScaleSlots;
         if (n >= kScaleSlots) wait(st.scales_free[slot], n / kScaleSlots - 1);
-        wait(st.sraw_full[slot], n / kScaleSlots);
+        wait_copy(st.sraw_full[slot], n / kScaleSlots);
         bool any = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
         for (int h = 0; h < NH; ++h) {
           if (t + 1 < tiles) {
             const unsigned slot = (n + 1) % C::NK, m = (n + 1) * NH + h;
-            wait(st.kraw_full[slot], (n + 1) / C::NK);
+            wait_copy(st.kraw_full[slot], (n + 1) / C::NK);
             if (m > 0) wait(st.k_free, m - 1);
             decode(std::integral_constant<int, KB>(), std::false_type(), h, C::off_raw + slot * C::kKeySlot, C::off_k, 0u);
             if (h == NH - 1) arrive(st.kraw_free[slot]);
@@ -531,7 +544,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) nq_attn_many_kernel(const AttnAr
           }
           if (t >= 0) {
             const unsigned slot = n % C::NV, ss = n % kScaleSlots, m = n * NH + h;
-            wait(st.vraw_full[slot], n / C::NV);
+            wait_copy(st.vraw_full[slot], n / C::NV);
             wait(st.scales_full[ss], n / kScaleSlots);
             if (m > 0) wait(st.v_free, m - 1);
             decode(std::integral_constant<int, VB>(), std::true_type(), h, C::off_raw_v + slot * C::kValueSlot, C::off_v, ss);
