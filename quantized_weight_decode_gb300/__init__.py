@@ -765,7 +765,9 @@ class KVCache:
         plan: attention_plan() of at least these sizes (made here if None,
         with the page table's width as the context's bound).  Returns (out bf16
         [total, q_heads, head_dim], lse fp32 [total, q_heads]): the tensors
-        given, else the plan's own, which its next call overwrites."""
+        given, else the plan's own, which its next call overwrites.  Rows of a
+        sequence whose starts the kernel finds wrong (last_device_error) are not
+        written: they hold what was there."""
         import torch
         qs = _heads_last(q, "attention")
         total, heads, dim = q.shape

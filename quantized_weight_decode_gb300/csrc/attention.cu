@@ -532,6 +532,8 @@ constexpr int64_t kFewKeys = 16384;
 // and 25.7 / 34.7.  Up to 16 k keys over all kv heads the many-rows kernel's
 // longer start decides, to 64 rows: one sequence of 2 k, 18 to 64 rows, 13.2 / 13.4 to
 // 15.7 / 16.5 (128), 13.5 / 18.8 to 16.0 / 27.0 (256), 11.1 / 12.6 to 12.9 / 15.7 (64).
+// (So for heads of 128 the two meet there; for 256 and 64 they would later, which
+// was not looked for: one rule for all.)
 bool takes_many(int rows, int dim, int64_t keys) {
   if (rows <= (dim == 64 ? 32 : 16)) return false;
   return rows > 64 || keys > kFewKeys;

@@ -35,9 +35,11 @@
 // thrashed the instruction cache (143 us against 94 for the same work).
 //
 // Measured (GB300): 8 sequences of up to 16 k keys, trees of up to 16, 40 query
-// heads of 128 on 8, 8 bits: 200 MB and 28.5 GFLOP in 85 us, of which the merge
-// takes 4 and the start and end of stretches about 10; the chain of hand-overs a
+// heads of 128 on 8, 8 bits: 200 MB and 28.5 GFLOP in 86 us, of which the merge
+// takes 4 and the start and end of stretches about 8; the chain of hand-overs a
 // tile bounds it (1.7 us a tile of 128 keys; with all arithmetic left out, 1.3).
+// One tree of 16 over 131 k keys, 24 query heads of 256 on 4: 210 MB in 162 us (two
+// row tiles, each decoding all codes).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
