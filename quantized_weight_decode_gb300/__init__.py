@@ -601,7 +601,8 @@ class AttentionPlan:
     none of their own (torch memory, kept by the plan, and beyond it until the
     streams of its calls are done with it).  Calls sharing a plan must be ordered
     (one stream), and each overwrites the outputs of the one before.  `stream`:
-    the stream of its calls, if that is not the current one."""
+    the stream of its calls, if that is not the current one.  A stream given by
+    its handle has to outlive the plan."""
 
     def __init__(self, seqs: int, max_drafts: int, q_heads: int, kv_heads: int, head_dim: int,
                  max_context: int, device="cuda", stream=None):
